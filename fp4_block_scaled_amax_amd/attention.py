@@ -38,12 +38,13 @@ def _rows16(x):
 
 
 def attention_layer(x, weights: dict, cache: dict, positions, page_table, lens, table, kv_workspace, heads: int,
-                    seq=None, cu_q=None, max_q: int = 1, interleaved: bool = False, causal: bool = True,
+                    seq=None, cu_q=None, max_q: int | None = None, interleaved: bool = False, causal: bool = True,
                     window: int = 0, ws=None, stream=None):
     """y [tokens][hidden] (bf16) from x [tokens][hidden] (bf16); the tokens'
     keys and values join the cache. Token t is token positions[t] of sequence
     seq[t] (None: of sequence t); lens holds the sequences' lengths with these
-    tokens, cu_q where each sequence's tokens begin (None: max_q of each)."""
+    tokens, cu_q where each sequence's tokens begin, at most max_q of each
+    (None: max_q, 1 by default, of each)."""
     torch = _torch()
     kv_heads, head_dim = cache["data"].shape[1], cache["data"].shape[3] // 18
     tokens = x.shape[0]

@@ -287,6 +287,8 @@ int nvfp4_kv_attention(const void* q, int dtype, int64_t total_q, int64_t heads,
     const int64_t tiles = ((max_q < total_q ? max_q : total_q) * (heads / kv_heads) + 127) / 128;
     if (batch > kMaxItems / kv_heads || tiles > kMaxItems / (batch * kv_heads))
         return NVFP4_ERR_SIZE;
+    if (total_q > batch * max_q)
+        return NVFP4_ERR_SHAPE;  // some sequence has more than max_q
     if ((st = strides_status(dtype, total_q, heads, head_dim, q_token_stride, q_head_stride)) != NVFP4_OK)
         return st;
     if (total_q == 0)

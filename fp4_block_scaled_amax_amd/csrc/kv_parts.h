@@ -24,35 +24,41 @@ __device__ __forceinline__ float2 get2(const float* p)
     return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
 }
 
-// Scalars of one sequence: its queries' rows in q, its visible tokens.
+// Scalars of one sequence: its queries' rows in q (the nq that are computed,
+// and `past` more than max_q allows), its visible tokens, and the position of
+// its first query. (pos0 is no less than -2^30: queries are fewer than that, so
+// one before the first token stays there, and no sum below passes 31 bits.)
 struct Seq {
     int64_t q0;
-    int nq, len;
+    int nq, past, len, pos0;
 };
 
 __device__ __forceinline__ Seq seq_of(const KvAttentionArgs& a, int b)
 {
     Seq s;
+    int64_t n = a.max_q;
     if (a.cu_q != nullptr) {
         s.q0 = a.cu_q[b];
         const int64_t end = min((int64_t)a.cu_q[b + 1], a.total_q);
-        s.nq = s.q0 < 0 ? 0 : (int)max((int64_t)0, min(end - s.q0, a.max_q));
+        n = s.q0 < 0 ? 0 : max((int64_t)0, end - s.q0);
     } else {
         s.q0 = b * a.max_q;
-        s.nq = (int)a.max_q;
     }
+    s.nq = (int)min(n, a.max_q);
+    s.past = (int)(n - s.nq);
     s.len = (int)max((int64_t)0, min((int64_t)a.lens[b], a.c.table_stride << a.c.page_shift));
+    s.pos0 = (int)max(s.len - n, -((int64_t)1 << 30));
     return s;
 }
 
 // Tokens [lo, hi) that query i of a sequence sees.
 __device__ __forceinline__ int first_seen(const KvAttentionArgs& a, const Seq& s, int i)
 {
-    return a.window > 0 ? max(0, s.len - s.nq + i - a.window + 1) : 0;
+    return a.window > 0 ? max(0, s.pos0 + i - a.window + 1) : 0;
 }
 __device__ __forceinline__ int end_seen(const KvAttentionArgs& a, const Seq& s, int i)
 {
-    return a.causal ? max(0, s.len - s.nq + i + 1) : s.len;
+    return a.causal ? max(0, s.pos0 + i + 1) : s.len;
 }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -98,6 +104,24 @@ __device__ __forceinline__ void write_row(const KvAttentionArgs& a, int64_t row,
         *reinterpret_cast<uint2*>(to) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
     if (a.lse != nullptr && d == 0)
         a.lse[row] = l == 0.0f ? neg_inf() : (m - kBias + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// NaN for the queries of a sequence that max_q leaves out (only the device knows
+// of them), by the workgroup that has the first rows of a kv head.
+template <class T, int D>
+__device__ __forceinline__ void write_past(const KvAttentionArgs& a, const Seq& s, int kv_head, int G, int threads)
+{
+    const float nan = __uint_as_float(0x7FC00000u);
+    const float v[8] = {nan, nan, nan, nan, nan, nan, nan, nan};
+    const int64_t units = (int64_t)s.past * G * (D / 8);
+    for (int64_t i = threadIdx.x; i < units; i += threads) {
+        const int64_t r = i / (D / 8), tok = r / G;
+        const int64_t row = (s.q0 + s.nq + tok) * a.heads + kv_head * G + (r - tok * G);
+        const int d = (int)(i % (D / 8)) * 8;
+        store8<T>(static_cast<char*>(a.out) + (row * D + d) * 2, v);
+        if (a.lse != nullptr && d == 0)
+            a.lse[row] = nan;
+    }
 }
 
 }  // namespace nvfp4

@@ -212,6 +212,8 @@ __global__ __launch_bounds__(64 * W) void kv_prompt_kernel(KvAttentionArgs a, in
     const Seq& s = piece.s;
     const int b = piece.b, kh = piece.kh, rows = piece.rows, r0 = piece.r0, r1 = piece.r1, parts = piece.parts;
     const int part = blockIdx.y;
+    if (s.past > 0 && part == 0 && r0 == 0)
+        write_past<T, D>(a, s, kh, G, 64 * W);
     if (r0 >= rows || part >= parts)
         return;
     const int seen_lo = piece.seen_lo, seen_hi = piece.seen_hi;

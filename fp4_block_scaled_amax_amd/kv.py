@@ -335,7 +335,7 @@ def nvfp4_kv_workspace(device=None):
     return torch.zeros(KV_WORKSPACE_BYTES // 4, dtype=torch.int32, device=device or "cuda")
 
 
-def nvfp4_kv_attention(q, cache, page_table, lens, workspace, cu_q=None, max_q: int = 1, scale: float | None = None,
+def nvfp4_kv_attention(q, cache, page_table, lens, workspace, cu_q=None, max_q: int | None = None, scale: float | None = None,
                        causal: bool = True, window: int = 0, out=None, return_lse: bool = False, lse=None,
                        stream=None):
     """Attention of q [total_q][heads][head_dim] (bfloat16 or float16; heads a
@@ -345,8 +345,8 @@ def nvfp4_kv_attention(q, cache, page_table, lens, workspace, cu_q=None, max_q: 
 
     lens: int32 [batch], the cached tokens of each sequence, the queries' own
     among them (they are appended first). cu_q: int32 [batch + 1], where each
-    sequence's queries begin, at most max_q each; None: max_q for every
-    sequence. Query i of n sits at position lens - n + i and sees the tokens
+    sequence's queries begin, at most max_q each (given with it; queries past
+    that are NaN); None: max_q (1 by default) for every sequence. Query i of n sits at position lens - n + i and sees the tokens
     up to itself (causal) and after its position - window (window > 0);
     without either all of them. One that sees nothing gives 0 and -inf.
     scale: 1 / sqrt(head_dim) by default. workspace: from nvfp4_kv_workspace,
@@ -354,6 +354,10 @@ def nvfp4_kv_attention(q, cache, page_table, lens, workspace, cu_q=None, max_q: 
     n = _n()
     tokens, h, d, *qs = _heads(n, q, "q")
     dt = _dtype(n, q.dtype, "q", f32=False)
+    if max_q is None:
+        if cu_q is not None:
+            raise ValueError("cu_q needs max_q, the most queries of one sequence")
+        max_q = 1
     dev = q.get_device()
     if _elsewhere(n, dev, stream):
         with _on(n, dev, stream):

@@ -161,8 +161,9 @@ int nvfp4_kv_read(const uint8_t* data, int64_t num_pages, int64_t kv_heads, int6
  *   q       [total_q][heads][head_dim] of dtype (BF16 or F16), strided
  *   cu_q    int32 [batch + 1]: sequence b has the queries cu_q[b] ..
  *           cu_q[b + 1] - 1, at most max_q; or NULL: max_q each (total_q =
- *           batch * max_q). It rises from 0 to total_q: rows of out that
- *           belong to no sequence are not written. The rows of a kv head that
+ *           batch * max_q). It rises from 0 to total_q (at most batch * max_q):
+ *           rows of out that belong to no sequence are not written. Queries of
+ *           a sequence past its first max_q give NaN (o and lse). The rows of a kv head that
  *           max_q allows choose the kernel (more than 32 to 128, by head_dim,
  *           are a prompt's), so prompts and single tokens go better in calls
  *           of their own.

@@ -220,3 +220,13 @@ def test_grids_that_no_launch_holds_are_refused(L):
     assert attention(b=1 << 23) == -6
     assert attention(n=1 << 20, mq=1 << 20, b=1 << 12) == -6
     assert attention(n=1 << 30, b=1 << 10, mq=1 << 20, cu=NULL) == -6
+
+
+def test_more_queries_than_max_q_allows_are_refused(L):
+    """With cu_q too, a call has at most max_q queries for each sequence."""
+    def f(n, mq, b=2, cu=A):
+        return L.nvfp4_kv_attention(A, 1, n, 4, 256, 64, cu, mq, A, 4, 2, 16, 64, A, A, A, b, 2, A, 0.125, 0, 1, A, NULL, A,
+                                    NULL)
+    assert f(5, 2) == -2
+    assert f(3, 1) == -2
+    assert f(1 << 30, (1 << 29) - 1) == -6        # a grid that no launch holds comes first
