@@ -207,6 +207,8 @@ int nvfp4_kv_append(const void* k, const void* v, int dtype, int64_t tokens,
         return NVFP4_ERR_ALIGN;
     if (heads > 0 && q == q_out && (q_token_stride != q_out_token_stride || q_head_stride != q_out_head_stride))
         return NVFP4_ERR_FLAGS;
+    if (seq == nullptr && tokens > batch)
+        return NVFP4_ERR_SHAPE;  // tokens of no sequence
     a.data = data;
     a.k = k;
     a.v = v;
@@ -253,6 +255,8 @@ int nvfp4_kv_read(const uint8_t* data, int64_t num_pages, int64_t kv_heads, int6
         return NVFP4_ERR_NULL;
     if (!aligned16(k_out) || !aligned16(v_out) || !aligned4(positions) || !aligned4(seq))
         return NVFP4_ERR_ALIGN;
+    if (seq == nullptr && tokens > batch)
+        return NVFP4_ERR_SHAPE;  // tokens of no sequence
     a.data = data;
     a.tokens = tokens;
     a.positions = positions;

@@ -249,9 +249,9 @@ def nvfp4_kv_append(cache, k, v, positions, page_table, seq=None, table=None, in
                     q_out=None, stream=None):
     """Quantizes k and v [tokens][kv_heads][head_dim] into the cache, k rotated
     on the way (table, as nvfp4_rope; None: not rotated). Token t is token
-    positions[t] of sequence seq[t] (int32; seq None: of sequence t), whose
-    pages are row seq[t] of page_table (int32 [batch][pages]). A negative
-    position marks padding. With q [tokens][heads][head_dim], also rotates the
+    positions[t] of sequence seq[t] (int32; seq None: of sequence t, at most
+    batch tokens), whose pages are row seq[t] of page_table (int32 [batch]
+    [pages]). A negative position marks padding. With q [tokens][heads][head_dim], also rotates the
     queries in the same launch and returns them (q_out: may be q itself);
     otherwise returns None."""
     n = _n()

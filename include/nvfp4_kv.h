@@ -113,7 +113,8 @@ int nvfp4_rope(const void* x, int dtype, int64_t tokens, int64_t heads, int64_t 
  *              position. A negative one marks padding: nothing is cached, and
  *              its row of q_out is zero.
  *   seq        int32 [tokens]: each token's sequence (row of page_table), or
- *              NULL: token t belongs to sequence t
+ *              NULL: token t belongs to sequence t (then tokens <= batch,
+ *              padding among them)
  *   page_table int32 [batch][table_stride]
  *   table      rotation table (max_pos, rot_dim as nvfp4_rope), or NULL with
  *              rot_dim 0: no rotation (then q must be NULL too)

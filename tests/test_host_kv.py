@@ -230,3 +230,16 @@ def test_more_queries_than_max_q_allows_are_refused(L):
     assert f(5, 2) == -2
     assert f(3, 1) == -2
     assert f(1 << 30, (1 << 29) - 1) == -6        # a grid that no launch holds comes first
+
+
+def test_tokens_of_no_sequence_are_refused(L):
+    """Without seq, token t belongs to sequence t: there are batch of them."""
+    def append(n, b, q=A, h=2):
+        return L.nvfp4_kv_append(A, A, 1, n, 128, 64, q, q, h, 128, 64, 128, 64, A, NULL, A, b, 2, A, 16, 32, 0, A, 4, 2,
+                                 16, 64, A, A, NULL)
+
+    def read(n, b):
+        return L.nvfp4_kv_read(A, 4, 2, 16, 64, A, A, n, A, NULL, A, b, 2, A, A, 1, NULL)
+    assert append(4, 3) == -2
+    assert append(2, 1, q=NULL, h=0) == -2
+    assert read(4, 3) == -2
