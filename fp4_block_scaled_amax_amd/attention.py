@@ -37,18 +37,35 @@ def _rows16(x):
     return padded
 
 
+def _sequences(seq, cu_q, max_q, tokens, batch, device):
+    """Each token's sequence as nvfp4_kv_append takes it, by what the attention
+    takes the tokens for: max_q of each sequence, or cu_q's."""
+    torch = _torch()
+    if cu_q is not None and max_q is None:
+        raise ValueError("cu_q needs max_q, the most tokens of one sequence")
+    if seq is not None or (max_q in (None, 1) and (cu_q is None or tokens == batch)):
+        return seq  # without it, one of each
+    at = torch.arange(tokens, dtype=torch.int32, device=device)
+    if cu_q is None:
+        return at // max_q
+    return torch.bucketize(at, cu_q[1:], out_int32=True, right=True)
+
+
 def attention_layer(x, weights: dict, cache: dict, positions, page_table, lens, table, kv_workspace, heads: int,
                     seq=None, cu_q=None, max_q: int | None = None, interleaved: bool = False, causal: bool = True,
                     window: int = 0, ws=None, stream=None):
     """y [tokens][hidden] (bf16) from x [tokens][hidden] (bf16); the tokens'
     keys and values join the cache. Token t is token positions[t] of sequence
-    seq[t] (None: of sequence t); lens holds the sequences' lengths with these
+    seq[t] (None: found from cu_q or max_q, by a torch kernel or two where a
+    sequence may have more than one; a program that runs many layers gives it);
+    lens holds the sequences' lengths with these
     tokens, cu_q where each sequence's tokens begin, at most max_q of each
     (None: max_q, 1 by default, of each)."""
     torch = _torch()
     kv_heads, head_dim = cache["data"].shape[1], cache["data"].shape[3] // 18
     tokens = x.shape[0]
     with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(x.device):
+        seq = _sequences(seq, cu_q, max_q, tokens, page_table.shape[0], x.device)
         ws = nvfp4_workspace(x.device) if ws is None else ws
         qkv = fprop(_rows16(x), weights["qkv"], ws=ws, out_dtype=torch.bfloat16)[:tokens]
         qkv = qkv.view(tokens, heads + 2 * kv_heads, head_dim)

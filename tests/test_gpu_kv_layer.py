@@ -116,3 +116,28 @@ def test_whole_prompt_equals_token_by_token(window):
     for o, d in zip(outs[1:], datas[1:]):
         assert torch.equal(d, datas[0])
         assert (o.float() - outs[0].float()).abs().max().item() <= 2 * (2.0 ** -11 + 2.0 ** -14 + 2.0 ** -8) * 8
+
+@pytest.mark.parametrize("cu", [False, True])
+def test_several_tokens_of_each_without_seq(cu):
+    """Without seq the tokens belong to the sequences as the attention takes
+    them: max_q of each, or by cu_q. The same outputs and cache as with it."""
+    hidden, heads, kv_heads, D, page, B = 256, 4, 2, 64, 16, 3
+    rng = np.random.default_rng(22)
+    w = F.layer.layer_weights(bf16(W.weight((heads + 2 * kv_heads) * D, hidden, seed=5)),
+                              bf16(W.weight(hidden, heads * D, seed=6)))
+    table, kws, ws = F.nvfp4_rope_table(64, D), F.nvfp4_kv_workspace(), F.nvfp4_workspace()
+    pages = i32([[7, 1, 2], [0, 4, 5], [3, 6, 8]])
+    for news in ([4, 4, 4], [1, 1, 1]) if not cu else ([2, 0, 5], [0, 1, 0], [1, 1, 0], [1, 1, 1]):
+        tokens = sum(news)
+        x = torch.from_numpy(rng.standard_normal((tokens, hidden)).astype(np.float32)).bfloat16().cuda()
+        pos = i32(np.concatenate([np.arange(9, 9 + k) for k in news]).tolist())
+        seq = i32(np.repeat(np.arange(B), news).tolist())
+        rest = dict(max_q=max(news), cu_q=i32(np.cumsum([0] + news).tolist()) if cu else None, ws=ws)
+        got = []
+        for s in (seq, None):
+            cache = F.nvfp4_kv_cache(9, kv_heads, D, 4.0, 4.0, page_size=page)
+            y = F.layer.attention_layer(x, w, cache, pos, pages, i32([9 + k for k in news]), table, kws, heads, seq=s, **rest)
+            got.append((y, cache["data"]))
+        assert got[0][1].any()
+        assert torch.equal(got[0][1], got[1][1])
+        assert torch.equal(got[0][0], got[1][0])

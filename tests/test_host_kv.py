@@ -243,3 +243,27 @@ def test_tokens_of_no_sequence_are_refused(L):
     assert append(4, 3) == -2
     assert append(2, 1, q=NULL, h=0) == -2
     assert read(4, 3) == -2
+
+
+def test_the_layer_finds_each_tokens_sequence():
+    """seq from max_q or cu_q, sequences without tokens among them; none where
+    every sequence has one token, and the given one as it is."""
+    import torch
+
+    from fp4_block_scaled_amax_amd.attention import _sequences
+
+    cpu = torch.device("cpu")
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
+    assert _sequences(None, None, None, 3, 3, cpu) is None
+    assert _sequences(None, None, 1, 3, 3, cpu) is None
+    assert _sequences(None, i32([0, 1, 2, 3]), 1, 3, 3, cpu) is None
+    given = i32([2, 0])
+    assert _sequences(given, i32([0, 1, 1, 2]), 1, 2, 3, cpu) is given
+    with pytest.raises(ValueError, match="max_q"):
+        _sequences(given, i32([0, 1, 1, 2]), None, 2, 3, cpu)
+    for news, max_q in (([4, 4, 4], 4), ([2, 0, 5], 5), ([0, 0, 3], 7), ([1, 0, 1], 1), ([0, 1, 0, 1, 1], 1)):
+        want = i32(np.repeat(np.arange(len(news)), news).tolist())
+        got = _sequences(None, i32(np.cumsum([0] + news).tolist()), max_q, sum(news), len(news), cpu)
+        assert got.dtype == torch.int32 and torch.equal(got, want)
+    got = _sequences(None, None, 4, 12, 3, cpu)
+    assert got.dtype == torch.int32 and torch.equal(got, i32([0, 0, 0, 0, 1, 1, 1, 1, 2, 2, 2, 2]))
