@@ -316,22 +316,16 @@ __global__ __launch_bounds__(64 * W) void kv_prompt_kernel(KvAttentionArgs a, in
         lds.nans = 0u;
     fetch(0);
 
-    // The rows in binary16 (a BF16 row scaled by a power of two, as in
-    // kv_stream.h).
+    // The rows in binary16 (a BF16 row scaled by a power of two, infinities NaN, as
+    // in kv_stream.h).
     f16x8 qf[D / 16];
     float f = a.scale * kLog2e * global_scale_from_amax(*a.c.k_amax);
     if constexpr (__is_same(T, Bf16)) {
-        uint32_t bits = 0u;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                bits = pk_max_u16(bits, word_at(raw_q[k], j) & 0x7FFF7FFFu);
-        const float top = halves_max(__uint_as_float(max(bits >> 16, bits & 0xFFFFu) << 16));
+        const float top = halves_max(__uint_as_float(top_bits(raw_q) << 16));
         int e = (int)((__float_as_uint(top) >> 23) & 255u) - 127;
         e = min(max(13 - e, -126), 126);
         const bool scale = top > 0.0f && top < __uint_as_float(0x7F800000u);
-        const float up = scale ? __uint_as_float((uint32_t)(e + 127) << 23) : 1.0f;
+        const float up = scale ? __uint_as_float((uint32_t)(e + 127) << 23) : top == 0.0f ? 1.0f : __uint_as_float(0x7FC00000u);
         f *= scale ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.0f;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
@@ -341,7 +335,7 @@ __global__ __launch_bounds__(64 * W) void kv_prompt_kernel(KvAttentionArgs a, in
     } else {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-            qf[k] = __builtin_bit_cast(f16x8, raw_q[k]);
+            qf[k] = nan_for_infinity(raw_q[k]);
     }
     float m = neg_inf(), l = 0.0f;
     floatx16 o[D / 32];

@@ -202,6 +202,30 @@ __device__ __forceinline__ void load_rows(RawRows<D, NT>& raw, const KvAttention
     }
 }
 
+// The largest |element| of 16-bit words, as its bits (their order is the
+// magnitudes'; a NaN's are above infinity's).
+template <int N>
+__device__ __forceinline__ uint32_t top_bits(const uint4 (&raw)[N])
+{
+    uint32_t bits = 0u;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            bits = pk_max_u16(bits, word_at(raw[k], j) & 0x7FFF7FFFu);
+    return max(bits >> 16, bits & 0xFFFFu);
+}
+
+// Infinite elements become NaN (x 0 + x): they leave no finite score, so that the
+// softmax is NaN; as -inf such scores would be taken for those of masked tokens.
+// (A row that sees nothing gives 0 all the same.) BF16 rows get their NaN with
+// their scaling.
+__device__ __forceinline__ f16x8 nan_for_infinity(uint4 raw)
+{
+    const f16x8 x = __builtin_bit_cast(f16x8, raw);
+    return __builtin_elementwise_fma(x, (f16x8)(_Float16)0.0f, x);
+}
+
 template <class T, int D, int NT>
 __device__ __forceinline__ void start_rows(Rows<D, NT>& w, const RawRows<D, NT>& raw, const KvAttentionArgs& a)
 {
@@ -213,17 +237,11 @@ __device__ __forceinline__ void start_rows(Rows<D, NT>& w, const RawRows<D, NT>&
             // The row is brought to binary16's range by a power of two that
             // puts its largest element into [2^13, 2^14): 8 bits fit down to
             // 2^-24. The inverse goes into the logits' factor.
-            uint32_t bits = 0u;  // two 15-bit maxima: the bit patterns' order is the magnitudes'
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    bits = pk_max_u16(bits, word_at(raw.v[n][k], j) & 0x7FFF7FFFu);
-            const float top = across16_max(__uint_as_float(max(bits >> 16, bits & 0xFFFFu) << 16));
+            const float top = across16_max(__uint_as_float(top_bits(raw.v[n]) << 16));
             int e = (int)((__float_as_uint(top) >> 23) & 255u) - 127;  // floor(log2) of a normal number
             e = min(max(13 - e, -126), 126);
             const bool scale = top > 0.0f && top < __uint_as_float(0x7F800000u);
-            const float up = scale ? __uint_as_float((uint32_t)(e + 127) << 23) : 1.0f;
+            const float up = scale ? __uint_as_float((uint32_t)(e + 127) << 23) : top == 0.0f ? 1.0f : __uint_as_float(0x7FC00000u);
             w.f[n] *= scale ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.0f;
 #pragma unroll
             for (int k = 0; k < D / 32; ++k)
@@ -233,7 +251,7 @@ __device__ __forceinline__ void start_rows(Rows<D, NT>& w, const RawRows<D, NT>&
         } else {
 #pragma unroll
             for (int k = 0; k < D / 32; ++k)
-                w.q[n][k] = __builtin_bit_cast(f16x8, raw.v[n][k]);
+                w.q[n][k] = nan_for_infinity(raw.v[n][k]);
         }
         w.m[n] = neg_inf();
         w.l[n] = 0.0f;

@@ -158,7 +158,8 @@ int nvfp4_kv_read(const uint8_t* data, int64_t num_pages, int64_t kv_heads, int6
  * the cached tokens t < lens[b], with NVFP4_KV_CAUSAL only t <= its position,
  * and with window > 0 only t > its position - window. Without NVFP4_KV_CAUSAL
  * every query sees all of them (cross attention to an encoder's states,
- * cached once). A query that sees nothing gives o = 0 and lse = -inf.
+ * cached once). A query that sees nothing gives o = 0 and lse = -inf; one with
+ * an infinite or NaN element that sees something gives NaN.
  *   q       [total_q][heads][head_dim] of dtype (BF16 or F16), strided
  *   cu_q    int32 [batch + 1]: sequence b has the queries cu_q[b] ..
  *           cu_q[b + 1] - 1, at most max_q; or NULL: max_q each (total_q =
