@@ -41,6 +41,28 @@ int strides_status(int dtype, int64_t tokens, int64_t heads, int64_t head_dim, i
     return NVFP4_OK;
 }
 
+// Whether two heads of a tensor that is written share elements: some token's
+// head begins less than head_dim from another's. Where the larger stride is past
+// all that the smaller one spans none does; otherwise its multiples are looked
+// at, each beside the nearest of the smaller's.
+bool overlaps(int64_t tokens, int64_t heads, int64_t head_dim, int64_t ts, int64_t hs)
+{
+    if (tokens <= 1 || heads <= 1)
+        return (tokens > 1 && ts < head_dim) || (heads > 1 && hs < head_dim);
+    const int64_t few = ts < hs ? ts : hs, n_few = ts < hs ? tokens : heads;
+    const int64_t far = ts < hs ? hs : ts, n_far = ts < hs ? heads : tokens;
+    if (few < head_dim)
+        return true;
+    if (far >= (n_few - 1) * few + head_dim)
+        return false;
+    for (int64_t k = 1; k < n_far && k * far / few < n_few; ++k) {
+        const int64_t past = k * far % few;
+        if (past < head_dim || (few - past < head_dim && k * far / few + 1 < n_few))
+            return true;
+    }
+    return false;
+}
+
 // The rotation's table: rot_dim elements of a head, rows below max_pos.
 int rope_status(int64_t head_dim, int64_t max_pos, int64_t rot_dim, uint32_t flags, uint32_t known)
 {
@@ -135,6 +157,8 @@ int nvfp4_rope(const void* x, int dtype, int64_t tokens, int64_t heads, int64_t 
     if ((st = strides_status(dtype, tokens, heads, head_dim, x_token_stride, x_head_stride)) != NVFP4_OK ||
         (st = strides_status(dtype, tokens, heads, head_dim, y_token_stride, y_head_stride)) != NVFP4_OK)
         return st;
+    if (overlaps(tokens, heads, head_dim, y_token_stride, y_head_stride))
+        return NVFP4_ERR_SHAPE;
     if (tokens == 0)
         return NVFP4_OK;
     if (x == nullptr || y == nullptr || positions == nullptr || table == nullptr)
@@ -198,6 +222,8 @@ int nvfp4_kv_append(const void* k, const void* v, int dtype, int64_t tokens,
         ((st = strides_status(dtype, tokens, heads, head_dim, q_token_stride, q_head_stride)) != NVFP4_OK ||
          (st = strides_status(dtype, tokens, heads, head_dim, q_out_token_stride, q_out_head_stride)) != NVFP4_OK))
         return st;
+    if (heads > 0 && overlaps(tokens, heads, head_dim, q_out_token_stride, q_out_head_stride))
+        return NVFP4_ERR_SHAPE;
     if (tokens == 0)
         return NVFP4_OK;
     if (k == nullptr || v == nullptr || positions == nullptr)

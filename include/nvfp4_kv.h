@@ -89,7 +89,8 @@ int nvfp4_rope_table(int64_t max_pos, int64_t rot_dim, double base, int scaling,
  * NVFP4_ROPE_ADJOINT takes -s for s: the transpose of the rotation, i.e. its
  * gradient (dx from dy), and its inverse where the amplitude is 1.
  *   x, y       [tokens][heads][head_dim] of dtype (F32, BF16 or F16); y may
- *              be x (same strides), otherwise they must not overlap
+ *              be x (same strides), otherwise they must not overlap; its heads
+ *              must not overlap each other either (x may be a broadcast view)
  *   positions  int32 [tokens]; one outside [0, max_pos) gives NaN in the
  *              rotated elements
  *   table      from nvfp4_rope_table (or the caller's own), 16-byte aligned
@@ -108,7 +109,7 @@ int nvfp4_rope(const void* x, int dtype, int64_t tokens, int64_t heads, int64_t 
  *   k, v       [tokens][kv_heads][head_dim] of dtype (F32, BF16 or F16), both
  *              with kv_token_stride and kv_head_stride
  *   q, q_out   [tokens][heads][head_dim] of dtype, or both NULL (heads 0);
- *              q_out may be q (same strides)
+ *              q_out may be q (same strides); as y of nvfp4_rope otherwise
  *   positions  int32 [tokens]: place in the sequence, and the rotation's
  *              position. A negative one marks padding: nothing is cached, and
  *              its row of q_out is zero.

@@ -267,3 +267,29 @@ def test_the_layer_finds_each_tokens_sequence():
         assert got.dtype == torch.int32 and torch.equal(got, want)
     got = _sequences(None, None, 4, 12, 3, cpu)
     assert got.dtype == torch.int32 and torch.equal(got, i32([0, 0, 0, 0, 1, 1, 1, 1, 2, 2, 2, 2]))
+
+
+def test_outputs_that_overlap_themselves_are_refused(L):
+    """A result whose tokens or heads share elements (a broadcast view) has no
+    value; any other strides are taken, nested or not (here up to the missing
+    input: nothing is launched)."""
+    def rope(n, h, d, ys):
+        return L.nvfp4_rope(NULL, 1, n, h, d, 0, 0, A, A, 16, 16, 0, A, *ys, NULL)
+
+    def append(n, h, ys):
+        return L.nvfp4_kv_append(NULL, A, 1, n, 128, 64, A, A, h, 64 * h, 64, *ys, A, A, A, 1, 2, A, 16, 32, 0, A, 4, 2, 16,
+                                 64, A, A, NULL)
+    rng = np.random.default_rng(5)
+    cases = [(4, 2, 64, (0, 64)), (4, 2, 64, (128, 0)), (4, 1, 64, (56, 0)), (1, 3, 64, (0, 32)), (4, 2, 64, (64, 64)),
+             (4, 3, 64, (128, 64)), (2, 4, 64, (64, 128)), (2, 2, 64, (192, 128)), (3, 3, 64, (192, 128)),
+             (1, 1, 64, (0, 0)), (5, 1, 64, (64, 0)), (4, 2, 64, (128, 64)), (4, 2, 64, (64, 256))]
+    cases += [(int(n), int(h), 16, (8 * int(a), 8 * int(b))) for n, h, a, b in rng.integers(1, 13, (400, 4))]
+    refused = 0
+    for n, h, d, ys in cases:
+        at = (np.arange(n)[:, None, None] * ys[0] + np.arange(h)[:, None] * ys[1] + np.arange(d)).reshape(-1)
+        apart = len(set(at.tolist())) == len(at)
+        refused += not apart
+        assert rope(n, h, d, ys) == (-1 if apart else -2), (n, h, d, ys)
+        if d == 64:
+            assert append(n, h, ys) == (-1 if apart else -2), (n, h, d, ys)
+    assert 100 < refused < len(cases) - 100
