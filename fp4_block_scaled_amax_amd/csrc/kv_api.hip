@@ -304,6 +304,8 @@ int nvfp4_kv_attention(const void* q, int dtype, int64_t total_q, int64_t heads,
     if ((dtype != NVFP4_BF16 && dtype != NVFP4_F16) || (flags & ~NVFP4_KV_CAUSAL) != 0 || !(scale > 0.0f) ||
         !isfinite(scale))
         return NVFP4_ERR_FLAGS;
+    if (batch == 0 && total_q == 0)
+        return NVFP4_OK;  // no sequences (and perhaps no page table)
     nvfp4::KvAttentionArgs a{};
     int st = cache_status(data, num_pages, kv_heads, page_size, head_dim, k_amax, v_amax, page_table, batch,
                           table_stride, a.c);

@@ -184,7 +184,8 @@ int nvfp4_kv_read(const uint8_t* data, int64_t num_pages, int64_t kv_heads, int6
  * power of two per head, which binary16 then holds exactly down to 2^-30 of
  * the head's largest element), softmax statistics and sums in binary32, the
  * weights p in binary16 (11 bits) for their products with the values.
- * scale: finite and positive. 1 <= max_q, total_q >= 0, batch >= 0.
+ * scale: finite and positive. 1 <= max_q, total_q >= 0, batch >= 0 (0: no
+ * sequences and no queries, nothing is done).
  */
 int nvfp4_kv_attention(const void* q, int dtype, int64_t total_q, int64_t heads,
                        int64_t q_token_stride, int64_t q_head_stride, const int32_t* cu_q,

@@ -293,3 +293,15 @@ def test_outputs_that_overlap_themselves_are_refused(L):
         if d == 64:
             assert append(n, h, ys) == (-1 if apart else -2), (n, h, d, ys)
     assert 100 < refused < len(cases) - 100
+
+
+def test_attention_of_no_sequences(L):
+    """An empty batch is nothing to do; queries of no sequence are refused."""
+    def f(n, b, pt=NULL, scale=0.125, cu=NULL):
+        return L.nvfp4_kv_attention(NULL, 1, n, 4, 256, 64, cu, 1, A, 4, 2, 16, 64, A, A, pt, b, 2, NULL, scale, 0, 1, NULL,
+                                    NULL, A, NULL)
+    assert f(0, 0) == 0
+    assert f(0, 0, pt=A, cu=A) == 0
+    assert f(0, 0, scale=-1.0) == -4
+    assert f(1, 0, pt=A) == -2
+    assert f(1, 0, pt=A, cu=A) == -2
