@@ -17,7 +17,7 @@ import contextlib
 import ctypes
 import math
 
-from . import BF16, F32, _check, _torch, lib
+from . import BF16, F32, Nvfp4Error, _check, _torch, lib
 
 F16 = 2  # a dtype beside F32 and BF16
 KV_WORKSPACE_BYTES = 64 << 20
@@ -234,8 +234,11 @@ def nvfp4_kv_cache(num_pages: int, kv_heads: int, head_dim: int, k_amax, v_amax,
     """An empty cache. k_amax, v_amax: the largest magnitudes that keys (after
     the rotation) and values are taken to have, as numbers or float32 [1]
     tensors (from nvfp4_amax of a calibration run); larger ones saturate.
-    page_size: a power of two from 16 on; head_dim: 64, 128 or 256."""
+    page_size: a power of two from 16 to 32768; head_dim: 64, 128 or 256."""
     torch = _torch()
+    if not 16 <= page_size <= 32768 or page_size & (page_size - 1) or head_dim not in (64, 128, 256):
+        raise Nvfp4Error(-2, f"a cache has pages of a power of two from 16 to 32768 tokens and heads of 64, 128 or 256 "
+                             f"elements, got {page_size} and {head_dim}")
     device = torch.device(device or "cuda")
 
     def amax(a):

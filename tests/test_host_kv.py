@@ -305,3 +305,13 @@ def test_attention_of_no_sequences(L):
     assert f(0, 0, scale=-1.0) == -4
     assert f(1, 0, pt=A) == -2
     assert f(1, 0, pt=A, cu=A) == -2
+
+
+def test_caches_that_no_call_takes_are_refused():
+    """A page of 24 tokens would become one of 16, at other places than the
+    caller's page table says."""
+    for page, d in ((24, 64), (0, 64), (8, 64), (-16, 64), (48, 128), (65536, 64), (16, 96), (16, 0)):
+        with pytest.raises(F.Nvfp4Error, match="ERR_SHAPE"):
+            F.nvfp4_kv_cache(2, 1, d, 8.0, 8.0, page_size=page, device="cpu")
+    cache = F.nvfp4_kv_cache(2, 3, 128, 8.0, 8.0, page_size=32, device="cpu")
+    assert cache["data"].shape == (2, 3, 2, 18 * 128)
