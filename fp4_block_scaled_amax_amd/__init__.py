@@ -150,6 +150,11 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _device(device):
+    """The device given (0 is the first GPU), or the current GPU."""
+    return _torch().device("cuda" if device is None else device)
+
+
 def _dev_tensor(t, name, dtype=None):
     torch = _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -197,7 +202,7 @@ def nvfp4_amax(x, rht: bool = False, rht_mask: int = 0, out=None, stream=None, b
 def nvfp4_workspace(device=None):
     """A zero-filled workspace for nvfp4_quantize_1d_fused."""
     torch = _torch()
-    return torch.zeros(WORKSPACE_BYTES // 4, dtype=torch.int32, device=device or "cuda")
+    return torch.zeros(WORKSPACE_BYTES // 4, dtype=torch.int32, device=_device(device))
 
 
 def _q1_outputs(x, rowwise, colwise, out):

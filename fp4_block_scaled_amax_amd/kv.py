@@ -17,7 +17,7 @@ import contextlib
 import ctypes
 import math
 
-from . import BF16, F32, Nvfp4Error, _check, _torch, lib
+from . import BF16, F32, Nvfp4Error, _check, _device, _torch, lib
 
 F16 = 2  # a dtype beside F32 and BF16
 KV_WORKSPACE_BYTES = 64 << 20
@@ -192,7 +192,7 @@ def nvfp4_rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, scaling:
     n = _n()
     if scaling not in _SCALINGS:
         raise ValueError(f"scaling must be one of {list(_SCALINGS)}")
-    device = n.torch.device(device or "cuda")
+    device = _device(device)
     if device.type == "cuda" and device.index is None:
         device = n.torch.device("cuda", n.torch.cuda.current_device())
     with _on(n, device.index, stream):
@@ -239,7 +239,7 @@ def nvfp4_kv_cache(num_pages: int, kv_heads: int, head_dim: int, k_amax, v_amax,
     if not 16 <= page_size <= 32768 or page_size & (page_size - 1) or head_dim not in (64, 128, 256):
         raise Nvfp4Error(-2, f"a cache has pages of a power of two from 16 to 32768 tokens and heads of 64, 128 or 256 "
                              f"elements, got {page_size} and {head_dim}")
-    device = torch.device(device or "cuda")
+    device = _device(device)
 
     def amax(a):
         return a if isinstance(a, torch.Tensor) else torch.full((1,), float(a), dtype=torch.float32, device=device)
@@ -335,7 +335,7 @@ def nvfp4_kv_read(cache, positions, page_table, seq=None, out_dtype=None, out=No
 def nvfp4_kv_workspace(device=None):
     """A zero-filled workspace for nvfp4_kv_attention."""
     torch = _torch()
-    return torch.zeros(KV_WORKSPACE_BYTES // 4, dtype=torch.int32, device=device or "cuda")
+    return torch.zeros(KV_WORKSPACE_BYTES // 4, dtype=torch.int32, device=_device(device))
 
 
 def nvfp4_kv_attention(q, cache, page_table, lens, workspace, cu_q=None, max_q: int | None = None, scale: float | None = None,

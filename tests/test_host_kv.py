@@ -315,3 +315,16 @@ def test_caches_that_no_call_takes_are_refused():
             F.nvfp4_kv_cache(2, 1, d, 8.0, 8.0, page_size=page, device="cpu")
     cache = F.nvfp4_kv_cache(2, 3, 128, 8.0, 8.0, page_size=32, device="cpu")
     assert cache["data"].shape == (2, 3, 2, 18 * 128)
+
+
+def test_device_0_is_the_first_gpu(monkeypatch):
+    """A device given as 0 is that one, not the current one."""
+    import torch
+
+    asked = []
+    monkeypatch.setattr(torch, "zeros", lambda *a, device=None, **k: asked.append(torch.device(device)))
+    for make in (F.nvfp4_workspace, F.nvfp4_kv_workspace, lambda d=None: F.nvfp4_kv_cache(
+            2, 1, 64, torch.ones(1), torch.ones(1), device=d)):
+        for given, want in ((0, "cuda:0"), (1, "cuda:1"), ("cuda:0", "cuda:0"), (None, "cuda"), (torch.device("cpu"), "cpu")):
+            make(given)
+            assert asked.pop() == torch.device(want)
