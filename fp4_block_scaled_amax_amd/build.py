@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(HERE, "libnvfp4.so")
 
 SOURCES = ["api.hip", "amax.hip", "quantize.hip", "rht_dequant.hip", "gemm.hip", "mx_quantize.hip",
            "mx_gemm.hip", "kv_api.hip", "rope.hip", "kv_cache.hip", "kv_attention.hip", "kv_prompt.hip"]
-HEADERS = ["device.h", "encode.h", "heads.h", "kernels.h", "kv_parts.h", "kv_stream.h", "quant_item.h"]
+HEADERS = ["device.h", "div_by.h", "encode.h", "heads.h", "kernels.h", "kv_parts.h", "kv_stream.h", "quant_item.h"]
 
 # Flags of single sources. kv_prompt.hip: products' accumulators in ordinary
 # registers (a 256-element head needs more than 256 of them, and the compiler

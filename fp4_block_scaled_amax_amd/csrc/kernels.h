@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "div_by.h"
+
 namespace nvfp4 {
 
 hipError_t launch_amax(const uint16_t* x, int64_t n, float* amax, hipStream_t stream);
@@ -100,29 +102,6 @@ hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream);
 // ---- key/value cache: rotary positions, append, read, attention
 
 enum { kF32 = 0, kBf16 = 1, kF16 = 2 };
-
-// Division of a 31-bit number by a constant of the launch: n / d =
-// (n * mul) >> 32 >> shift, exact for n < 2^31 (mul = ceil(2^(32 + shift) /
-// d) with 2^shift >= d; then mul d - 2^(32 + shift) < d <= 2^shift, and the
-// error n (mul d - 2^(32 + shift)) / (d 2^(32 + shift)) stays below 1 / d).
-struct DivBy {
-    uint32_t d;
-    uint64_t mul;
-    uint32_t shift;
-
-    static DivBy of(uint32_t d)
-    {
-        uint32_t s = 0;
-        while (((uint64_t)1 << s) < d)
-            ++s;
-        const uint64_t one = (uint64_t)1 << s;
-        // ceil(2^32 * 2^s / d) in 64 bits: s <= 31
-        return DivBy{d, ((one << 32) + d - 1) / d, s};
-    }
-#if defined(__HIPCC__)
-    __device__ __forceinline__ uint32_t div(uint32_t n) const { return (uint32_t)(((uint64_t)n * mul) >> 32 >> shift); }
-#endif
-};
 
 struct RopeTableArgs {
     int64_t max_pos;

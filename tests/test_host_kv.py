@@ -328,3 +328,53 @@ def test_device_0_is_the_first_gpu(monkeypatch):
         for given, want in ((0, "cuda:0"), (1, "cuda:1"), ("cuda:0", "cuda:0"), (None, "cuda"), (torch.device("cpu"), "cpu")):
             make(given)
             assert asked.pop() == torch.device(want)
+
+
+def test_the_kernels_division_by_a_launch_constant(tmp_path):
+    """The same with csrc/div_by.h itself, compiled for the host: every divisor
+    up to 4096, powers of two and their neighbours, and large ones, at both ends
+    of quotient steps from the first to the last."""
+    import os
+    import subprocess
+
+    source, program = tmp_path / "div.cpp", tmp_path / "div"
+    source.write_text(r"""
+#include <stdio.h>
+#include <initializer_list>
+#include "div_by.h"
+static uint64_t seed = 1;
+static uint64_t draw() { return (seed = seed * 6364136223846793005ull + 1442695040888963407ull) >> 33; }  // 31 bits
+static int wrong = 0;
+static void check(uint32_t d)
+{
+    const nvfp4::DivBy by = nvfp4::DivBy::of(d);
+    const uint64_t last = 0x7FFFFFFFull / d;
+    auto at = [&](uint64_t q) {
+        for (uint64_t n : {q * d - 1, q * d, q * d + 1, q * d + d - 1})
+            if (n <= 0x7FFFFFFFull && by.div((uint32_t)n) != n / d && wrong++ < 5)
+                printf("%llu / %u: %u\n", (unsigned long long)n, d, by.div((uint32_t)n));
+    };
+    for (uint64_t q = 0; q < 8; ++q) {
+        at(q);
+        at(last - (q < last ? q : last));
+    }
+    for (int i = 0; i < 32; ++i)
+        at(draw() % (last + 1));
+}
+int main()
+{
+    for (uint32_t d = 1; d <= 4096; ++d)
+        check(d);
+    for (uint32_t b = 2; b < 31; ++b)
+        for (int i = -1; i <= 1; ++i)
+            check((1u << b) + i);
+    for (int i = 0; i < 20000; ++i)
+        check((uint32_t)(draw() >> (i % 20)) + 1);
+    printf("%d wrong\n", wrong);
+    return wrong != 0;
+}
+""")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-I", os.path.join(os.path.dirname(B.__file__), "csrc"), "-o",
+                    str(program), str(source)], check=True)
+    done = subprocess.run([str(program)], capture_output=True, text=True, timeout=60)
+    assert done.returncode == 0 and done.stdout == "0 wrong\n", done.stdout
