@@ -236,7 +236,8 @@ __device__ __forceinline__ void start_rows(Rows<D, NT>& w, const RawRows<D, NT>&
         if constexpr (__is_same(T, Bf16)) {
             // The row is brought to binary16's range by a power of two that
             // puts its largest element into [2^13, 2^14): 8 bits fit down to
-            // 2^-24. The inverse goes into the logits' factor.
+            // 2^-17, that is 2^-30 of the largest; smaller elements are rounded
+            // to multiples of 2^-24. The inverse goes into the logits' factor.
             const float top = across16_max(__uint_as_float(top_bits(raw.v[n]) << 16));
             int e = (int)((__float_as_uint(top) >> 23) & 255u) - 127;  // floor(log2) of a normal number
             e = min(max(13 - e, -126), 126);
