@@ -8,9 +8,11 @@ projections around attention over an NVFP4 key/value cache.
   y = o Wo^T           linear.fprop
 
 The same call takes a decode step (one token of each sequence), several
-drafted tokens of each, a prompt, a chunk of one, or a mixture (cu_q). Every
-step runs in the library's kernels; this module only sequences calls on one
-stream. What a serving program keeps between calls is made once: the weights
+drafted tokens of each, a prompt, a chunk of one, or a mixture (cu_q; every
+sequence then takes the kernel that max_q asks for, so that prompts and single
+tokens go faster in calls of their own). The four steps run in the library's
+kernels; around them torch fills and copies x and o up to a multiple of 16
+tokens where they are not one, and finds seq where it is not given. What a serving program keeps between calls is made once: the weights
 (layer_weights), the cache (nvfp4_kv_cache), the rotation table
 (nvfp4_rope_table) and two workspaces (nvfp4_workspace, nvfp4_kv_workspace).
 """

@@ -164,8 +164,8 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppendArgs a, int
 }
 
 // The same tiling: one 16-element block per thread, decoded as
-// nvfp4_dequantize does. 8192 tokens of 2 x 8 heads of 128 to bf16: 10.3 us
-// (43 MB, 4.2 TB/s).
+// nvfp4_dequantize does. 8192 tokens of 2 x 8 heads of 128 to bf16: 10.4 to
+// 11.4 us (43 MB, 3.8 to 4.1 TB/s).
 template <class T, int D>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadArgs a)
 {

@@ -25,11 +25,11 @@
 // h - 1, all in one stretch of code without a branch. Steps at the edges
 // (masked, first, last) take the same operations one after the other.
 //
-// The products bound it. 8192 tokens, 32 heads of 128 over 8, causal: 513 us
-// (539 on another card), 1.07 PFLOP/s of the pairs that are seen (a large library matrix product
+// The products bound it. 8192 tokens, 32 heads of 128 over 8, causal: 508 to 539
+// us by card, 1.02 to 1.08 PFLOP/s of the pairs that are seen (a large library matrix product
 // reaches 1.36 in bf16 and 1.22 in f16), matrix cores and vector units busy in
 // 52 % of the cycles each, at the 1.9 GHz that the power allows; 2048 tokens
-// over 8192: 235 us, 1.02 PFLOP/s (one workgroup for each compute unit, whose
+// over 8192: 231 to 251 us, 0.96 to 1.04 PFLOP/s (one workgroup for each compute unit, whose
 // rows see 6144 to 8192 tokens: the last are waited for); 4096 tokens, 16 heads
 // of 256: 172 us, 800 TFLOP/s. The same products, loads and weights one after
 // the other took 700 us for the first.

@@ -46,8 +46,9 @@ __global__ __launch_bounds__(kThreads) void rope_table_kernel(RopeTableArgs a)
 // caches. The split into token, head and unit is one multiplication each (a
 // division by a launch constant).
 //
-// Measured: 8192 tokens x 32 heads x 128, bf16 26.3 us a call from memory (5.3
-// TB/s; a large copy reaches 5.05); 4095 x 16 x 256 binary32, 64 elements rotated, 27.6 us (4.9 TB/s); 64
+// Measured: 8192 tokens x 32 heads x 128, bf16 26.3 to 28 us a call, by card, with
+// six inputs in turn, which then come from memory (4.8 to 5.1 TB/s; a large copy
+// reaches 5.05), 22 to 24 with two, which the last-level cache holds in part; 4095 x 16 x 256 binary32, 64 elements rotated, 27.6 us (4.9 TB/s); 64
 // tokens 3.0 us, an empty launch 2.3.
 template <class T>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, int64_t token0, uint32_t units, bool stream_y)
@@ -98,7 +99,7 @@ hipError_t launch_rope(const RopeArgs& a, hipStream_t stream)
     const int64_t most = ((int64_t)1 << 30) / per_token;
     // A result larger than the XCDs' L2s (8 x 4 MiB) is written past them: it
     // would only be pushed out, at the launch's end. Whole lines are, that is,
-    // 16-bit heads of 128 and more, aligned. (26.3 us where the caches take
+    // 16-bit heads of 128 and more, aligned. (From memory: 26.3 us where the caches take
     // 27.7, 27.4 and 28.3 with neighbouring pairs; heads of 64 elements alike;
     // binary32, whose threads write half lines, 70 and 27.)
     const int64_t head_dim = 16 * (int64_t)a.by_units.d;
